@@ -38,14 +38,14 @@ def listed():
         _few("few_mixtral_t1", 1, 4096, 8, 2, 14336, "bf16"),
         # a decode batch of eight over the same weights in fp8
         _few("few_mixtral_t8_fp8", 8, 4096, 8, 2, 14336, "fp8_e4m3"),
-        # the most tokens the call takes: every expert touched
-        _few("few_mixtral_t16", 16, 4096, 8, 2, 14336, "bf16"),
+        # the benchmark's decode batch: every expert touched
+        _few("few_mixtral_t64", 64, 4096, 8, 2, 14336, "bf16"),
         # fine-grained layer with its shared expert and device-limited routing, a
         # ragged batch, 4-bit weights
         _few("few_fine_t13_int4", 13, 7168, 256, 8, 2048, "int4", shared=True, groups=8,
              topk_groups=4),
         # a small layer whose capacity drops assignments to the shared expert
-        _few("few_small_t11_int8", 11, 768, 32, 8, 256, "int8", shared=True, cf=0.75,
+        _few("few_small_t37_int8", 37, 768, 32, 8, 256, "int8", shared=True, cf=0.75,
              overflow="shared", bias=True),
         # one request's next token through an attention-output-sized projection
         _adapter("adapter_t1", 1, 4096, 4096, 32, 16, "bf16", "bf16", "scattered"),
@@ -97,7 +97,7 @@ def draw(rng):
             cf = rng.choice([0.0, 0.0, 0.5, 1.25])
             overflow = rng.choice(["drop", "shared"]) if shared and cf else "drop"
             # quantised matrices hold a scale per 128 rows
-            c = _few("", _log_int(rng, 1, 16),
+            c = _few("", _log_int(rng, 1, 64),
                      _log_int(rng, 256, 7168, 64 if w == "bf16" else 128), E,
                      rng.randint(1, kmax), _log_int(rng, 128, 14336, 128), w, shared, groups, tg,
                      cf, overflow, rng.random() < 0.3)
