@@ -14,8 +14,8 @@
  *   moe_combine     weighted sum of each token's k grouped outputs
  *   moe_forward     all of the above on one stream, no host synchronisation
  *
- * and, for serving, moe_forward_few: the same layer for 1 to 16 tokens in two
- * launches, and moe_adapter_linear: low-rank adapters of many requests beside
+ * and, for serving, moe_forward_few: the same layer for 1 to 64 tokens (to 16 of
+ * them in two launches), and moe_adapter_linear: low-rank adapters of many requests beside
  * a shared projection (the one that feeds the layer) or beside the layer.
  *
  * Conventions shared by every entry point
@@ -341,21 +341,24 @@ moe_status moe_forward_noalloc(const moe_shape* shape, const void* x, const floa
                                int32_t* offsets, void* stream);
 
 /* Most tokens moe_forward_few takes. */
-#define MOE_FEW_MAX_TOKENS 16
+#define MOE_FEW_MAX_TOKENS 64
 
 /* Bytes of device workspace moe_forward_few needs for `shape` [host]; 0 when
- * moe_forward_few does not take the shape (moe_last_error() says why). */
+ * moe_forward_few does not take the shape (moe_last_error() says why).  It does not
+ * shrink as T grows: a workspace for the largest batch serves every smaller one of an
+ * otherwise equal shape. */
 size_t moe_few_workspace_bytes(const moe_shape* shape);
 
-/* The whole layer for a few tokens, 0 <= T <= MOE_FEW_MAX_TOKENS, in two
- * launches (route; select, group, gate/up, down and combine): the same stages,
+/* The whole layer for a few tokens, 0 <= T <= MOE_FEW_MAX_TOKENS: the same stages,
  * arguments and outputs as moe_forward, for single tokens and decode batches,
  * where the layer is the stream of the touched experts' weights and
- * moe_forward's launches and row tiles cost as much again.  It is the faster call
+ * moe_forward's launches and row tiles cost as much again.  Up to 16 tokens take two
+ * launches (route; select, group, gate/up, down and combine), more take moe_forward's
+ * route, dispatch and grouped combine with two launches of the experts between.  It is the faster call
  * for narrow experts and for quantised weights (one token, 64 experts of 1408: 39 us
  * against 110; 16 tokens, Mixtral-shaped, int4: 239 against 241); wide bf16 experts
  * are read faster by moe_forward (one token 143 us against 152, 16 tokens 459
- * against 570).
+ * against 570, 64 tokens 471 against 775).
  *   - SwiGLU experts in every weight type, group-limited routing, a shared
  *     expert, the capacity with MOE_OVERFLOW_DROP and MOE_OVERFLOW_SHARED.
  *     MOE_ERR_UNSUPPORTED: more tokens, Linear+bias experts,

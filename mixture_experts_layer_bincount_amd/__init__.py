@@ -295,7 +295,7 @@ def moe_forward_noalloc(shape, x, W_g, b_g, weights, y, topk_idx, topk_w, counts
                                     _stream(stream)))
 
 
-FEW_MAX_TOKENS = 16  # MOE_FEW_MAX_TOKENS
+FEW_MAX_TOKENS = 64  # MOE_FEW_MAX_TOKENS
 
 
 def moe_few_workspace_bytes(shape: Shape) -> int:
@@ -312,7 +312,7 @@ def few_workspace(shape: Shape, device="cuda") -> torch.Tensor:
 
 def moe_forward_few(shape, x, W_g, b_g, weights, y, topk_idx, topk_w, counts, offsets, ws,
                     stream=None):
-    """The whole layer for at most FEW_MAX_TOKENS tokens, in two launches."""
+    """The whole layer for at most FEW_MAX_TOKENS tokens."""
     _check(_lib.moe_forward_few(ctypes.byref(shape), _ptr(x), _ptr(W_g), _ptr(b_g),
                                 ctypes.byref(weights), _ptr(y), _ptr(topk_idx), _ptr(topk_w),
                                 _ptr(counts), _ptr(offsets), _ptr(ws), _stream(stream)))

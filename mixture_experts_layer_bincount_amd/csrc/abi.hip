@@ -456,10 +456,12 @@ namespace moe {
 namespace {
 
 // The layer's launch sequence over a workspace `ws` of ws_layout(*shape)
-// bytes.  `timed`: record the stage events when stage timing is enabled.
+// bytes.  `timed`: record the stage events when stage timing is enabled.  `few_H`: the
+// experts by launch_few_rows, its hidden rows there (grouped combine).
 moe_status forward_impl(const moe_shape* shape, const void* x, const float* W_g, const float* b_g,
                         const moe_weights* w, float* y, int32_t* topk_idx, float* topk_w,
-                        int32_t* counts, int32_t* offsets, void* ws, void* stream, bool timed) {
+                        int32_t* counts, int32_t* offsets, void* ws, void* stream, bool timed,
+                        void* few_H = nullptr) {
   MOE_TRY(check_shape(shape, true));
   const moe_shape& s = *shape;
   if (s.E > 256 && !router_mfma_epad(s))
@@ -520,8 +522,9 @@ moe_status forward_impl(const moe_shape* shape, const void* x, const float* W_g,
   if (L.grouped_combine) {
     // grouped fp32 output, then the combine kernel writes every element of y
     ce.mark(4, st);
-    MOE_TRY(hip_status(launch_expert_ffn(s, L, *w, x, offsets, W.perm_token, W.perm_w, W.Yp,
-                                         nullptr, W.H, st, ce.at(5)),
+    MOE_TRY(hip_status(few_H ? launch_few_rows(s, L, *w, x, offsets, W.perm_token, few_H, W.Yp, st)
+                             : launch_expert_ffn(s, L, *w, x, offsets, W.perm_token, W.perm_w, W.Yp,
+                                                 nullptr, W.H, st, ce.at(5)),
                        "expert ffn"));
     const moe_status r = hip_status(
         launch_combine(s, L.P_max, W.Yp, W.slot_pos, topk_w, y, st), "combine");
@@ -569,6 +572,17 @@ hipError_t scratch_address(void** out) {
   if (g_scratch.err[dev] != hipSuccess) return g_scratch.err[dev];
   *out = g_scratch.ptr[dev];
   return hipSuccess;
+}
+
+// moe_forward_few past kFewColumns tokens: the layer's own route, dispatch and grouped
+// combine around few_rows.hip's experts, over this shape's workspace and, behind it,
+// the hidden rows.
+moe_shape few_grouped(const moe_shape& shape, int64_t T) {
+  moe_shape s = shape;
+  s.T = T;
+  s.combine = MOE_COMBINE_GROUPED;
+  s.hidden_split = 0;
+  return s;
 }
 
 // What moe_forward_few takes.
@@ -620,7 +634,16 @@ extern "C" {
 
 size_t moe_few_workspace_bytes(const moe_shape* shape) {
   if (check_few(shape) != MOE_OK) return 0;
-  return few_workspace_bytes(*shape);
+  // (fewer tokens never need more: one workspace serves every smaller batch)
+  moe_shape s = *shape;
+  s.T = std::min<int64_t>(s.T, kFewColumns);
+  size_t most = few_workspace_bytes(s);
+  for (int64_t T = kFewColumns + 1; T <= shape->T; ++T) {
+    const moe_shape g = few_grouped(*shape, T);
+    const WsLayout L = ws_layout(g);
+    most = std::max(most, L.total + few_rows_bytes(g, L.H_rows));
+  }
+  return most;
 }
 
 moe_status moe_forward_few(const moe_shape* shape, const void* x, const float* W_g,
@@ -648,6 +671,11 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const float* W
       MOE_TRY(check_ptr(w->W3s, "W3s", 16));
       MOE_TRY(check_ptr(w->W2s, "W2s", 16));
     }
+  }
+  if (s.T > kFewColumns) {
+    const moe_shape g = few_grouped(s, s.T);
+    return forward_impl(&g, x, W_g, b_g, w, y, topk_idx, topk_w, counts, offsets, ws, stream,
+                        /*timed=*/false, (char*)ws + ws_layout(g).total);
   }
   const moe_weights none{};
   return hip_status(launch_forward_few(s, x, W_g, b_g, w ? *w : none, y, topk_idx, topk_w, counts, offsets, ws,

@@ -59,16 +59,6 @@ __device__ __forceinline__ int adapter_rank(const AdapterParams& p, int a) {
   return p.ranks ? max(0, min(p.ranks[a], p.R)) : p.R;
 }
 
-// Three bf16 terms of a value (24 bits; a value past bf16's range keeps its
-// first term).
-__device__ __forceinline__ void split3(float v, uint32_t& h, uint32_t& m, uint32_t& l) {
-  h = f32_to_bf16_bits(v);
-  float rest = v - bf16_bits_to_f32(h);
-  if ((h & 0x7F80u) == 0x7F80u) rest = 0.f;
-  m = f32_to_bf16_bits(rest);
-  l = f32_to_bf16_bits(rest - bf16_bits_to_f32(m));
-}
-
 // ---------------------------------------------------------------- shrink
 // One 16-row tile of x against 16 rows of every adapter that the tile's rows
 // name (each once); Z workgroups take the adapters in turn, KS of them split

@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kWaves = 8;             // waves of a workgroup
 constexpr int kThreads = kWaves * 64;
-constexpr int kCols = 16;             // tokens of a call at most
+constexpr int kCols = kFewColumns;    // tokens of a call at most
 // Output rows of a down item (the last may have 64 of 128).  Eight row tiles share
 // each load of h: with four, the loads of its three terms cost as much as narrow
 // weights' (16 tokens, int4, Mixtral widths: 266 us against 251); bf16 weights are
@@ -48,7 +48,6 @@ constexpr int kDownRowsMin = 64;
 constexpr int down_rows(int wq) { return wq == WS_BF16 ? kDownRowsMin : 128; }
 constexpr int kMaxSplits = 8;         // K splits of the router at most
 constexpr int kMaxPieces = 16;        // k pieces the down items of a row tile are cut into
-static_assert(kCols == MOE_FEW_MAX_TOKENS, "tokens are MFMA columns");
 
 struct FewParams {
   const uint16_t* x;      // [T, d]

@@ -151,12 +151,20 @@ hipError_t launch_combine(const moe_shape& s, int64_t P_max, const float* y_perm
                           const int32_t* slot_pos, const float* topk_w, float* y,
                           hipStream_t st);
 
-// The whole layer for at most MOE_FEW_MAX_TOKENS tokens over a workspace of
+// The whole layer for at most kFewColumns tokens over a workspace of
 // few_workspace_bytes(s) bytes.
+constexpr int kFewColumns = 16;  // tokens as the columns of one MFMA tile
 size_t few_workspace_bytes(const moe_shape& s);
 hipError_t launch_forward_few(const moe_shape& s, const void* x, const float* W_g, const float* b_g,
                               const moe_weights& w, float* y, int32_t* topk_idx, float* topk_w,
                               int32_t* counts, int32_t* offsets, void* ws, hipStream_t st);
+
+// The experts of a few more tokens (up to 64 rows an expert) into the grouped output
+// y_perm, over few_rows_bytes(s, L.H_rows) bytes of hidden rows.
+size_t few_rows_bytes(const moe_shape& s, int64_t H_rows);
+hipError_t launch_few_rows(const moe_shape& s, const WsLayout& L, const moe_weights& w,
+                           const void* x, const int32_t* offsets, const int32_t* perm_token,
+                           void* H, float* y_perm, hipStream_t st);
 
 // Low-rank adapters beside a shared projection, over a workspace of
 // adapter_workspace_bytes(s) bytes; T > 0.

@@ -124,6 +124,16 @@ __device__ __forceinline__ bf16x8 widen(const u32x4& q, int i) {
   }
 }
 
+// Three bf16 terms of a value (24 bits; a value past bf16's range keeps its
+// first term).
+__device__ __forceinline__ void split3(float v, uint32_t& h, uint32_t& m, uint32_t& l) {
+  h = f32_to_bf16_bits(v);
+  float rest = v - bf16_bits_to_f32(h);
+  if ((h & 0x7F80u) == 0x7F80u) rest = 0.f;
+  m = f32_to_bf16_bits(rest);
+  l = f32_to_bf16_bits(rest - bf16_bits_to_f32(m));
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // A raw buffer over [ptr, ptr + bytes), bytes < 2^31, from values that are the
