@@ -685,6 +685,7 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const float* W
 
 size_t moe_adapter_workspace_bytes(const moe_adapter_shape* shape) {
   if (check_adapter(shape) != MOE_OK) return 0;
+  if (shape->T == 0) return 256;  // (nothing is launched, and no plan is made)
   return std::max<size_t>(adapter_workspace_bytes(*shape), 256);
 }
 
