@@ -394,7 +394,9 @@ typedef struct moe_adapter_shape {
 } moe_adapter_shape;
 
 /* Bytes of device workspace moe_adapter_linear needs for `shape` [host]; 0
- * when it does not take the shape (moe_last_error() says why). */
+ * when it does not take the shape (moe_last_error() says why).  It does not shrink
+ * as T grows: a workspace for the largest batch serves every smaller one of an
+ * otherwise equal shape. */
 size_t moe_adapter_workspace_bytes(const moe_adapter_shape* shape);
 
 /* A projection shared by all rows plus each row's own low-rank adapter:

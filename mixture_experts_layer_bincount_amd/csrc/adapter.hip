@@ -733,9 +733,20 @@ hipError_t launch_weights(const moe_adapter_shape& s, const AdapterParams& p, co
 
 }  // namespace
 
-size_t adapter_workspace_bytes(const moe_adapter_shape& s) {
-  const Plan q = plan_of(s, true), bare = plan_of(s, false);
-  return std::max(s_bytes(s, q) + (size_t)q.KW * s.T * s.d_out * 4, s_bytes(s, bare));
+// The most that any batch of 1 .. s.T rows takes: few rows' products are cut into parts
+// that many rows' are not, and a workspace made for the largest batch is to serve them
+// all.  From 16 rows on a plan changes only between multiples of 16; once W takes the
+// 256 x 256 tiles (no parts) and S is in one part, more rows just have more of S.
+size_t adapter_workspace_bytes(const moe_adapter_shape& shape) {
+  moe_adapter_shape s = shape;
+  size_t most = 0;
+  for (int64_t T = 1; T < shape.T + 16; T += T < 16 ? 1 : 16) {
+    s.T = std::min(T, shape.T);
+    const Plan q = plan_of(s, true), bare = plan_of(s, false);
+    most = std::max({most, s_bytes(s, q) + (size_t)q.KW * s.T * s.d_out * 4, s_bytes(s, bare)});
+    if (q.BM == 256 && q.KS == 1 && bare.KS == 1) break;
+  }
+  return std::max(most, align256((size_t)shape.T * shape.rank * 4));
 }
 
 hipError_t launch_adapter_linear(const moe_adapter_shape& s, const void* x, const void* W,

@@ -26,3 +26,25 @@ def test_layer_of_no_tokens_with_adapters(moe, few):
     layer = moe.MoELayer(0, 64, 4, 2, 128, W_g=None, weights={}, device="cpu", pack_router=False,
                          few=few, adapters=ad)
     assert layer.adapter_ws.numel() == 256 and layer.y.shape == (0, 64)
+
+
+def sizes(moe, rows, **kw):
+    return [moe.moe_adapter_workspace_bytes(moe.make_adapter_shape(T, **kw)) for T in rows]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(d_in=4096, d_out=4096, n_adapters=8, rank=16),
+    dict(d_in=4096, d_out=14336, n_adapters=8, rank=16),
+    dict(d_in=7168, d_out=2048, n_adapters=8, rank=64, w_dtype=4),
+    dict(d_in=512, d_out=100, n_adapters=3, rank=128),
+    dict(d_in=8, d_out=1, n_adapters=1, rank=8),
+    dict(d_in=8192, d_out=1 << 15, n_adapters=1, rank=8)])
+def test_workspace_serves_smaller_batches(moe, kw):
+    """Never smaller for more rows: a workspace for the largest batch is enough for every
+    smaller one, whatever parts the products of those are cut into."""
+    rows = [*range(0, 1100), *range(1100, 9000, 37), *range(9000, 1 << 20, 4999), 1 << 20]
+    rows = [T for T in rows if T * kw["d_out"] <= 1 << 37]
+    got = sizes(moe, rows, **kw)
+    assert got[0] > 0
+    down = [(a, b) for a, b, x, y in zip(rows, rows[1:], got, got[1:]) if y < x]
+    assert not down, down[:5]
