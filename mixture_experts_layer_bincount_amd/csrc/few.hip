@@ -651,8 +651,18 @@ __device__ __forceinline__ void down_item(const FewParams& p, const FewLds& L, Q
       }
     };
     const uint32_t wlane = (uint32_t)(r * rowb) + map.lane_w(g), plane = (uint32_t)p.d_ff * 2u;
+    // A column without the segment keeps its sum: its products are zeros times the
+    // weights, which need not be finite.
+    const bool own = (sg.tokens >> r) & 1;
     if constexpr (WQ == WS_BF16) {
+      f32x4 kept[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) kept[i] = sum[i][0];
       stream_rows<WQ, RT, 1, 3, PD, kLoadAgent>(map, wr, wlane, hr, aoff, plane, share, sum, ready);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum[i][0][c] = own ? sum[i][0][c] : kept[i][c];
     } else {
       f32x4 acc[RT][1];
       zero_frags(acc);
@@ -660,7 +670,10 @@ __device__ __forceinline__ void down_item(const FewParams& p, const FewLds& L, Q
       const float sc = kWeightUnit<WQ> *
                        (sg.e < 0 ? p.s2s[nt] : p.s2[(int64_t)sg.e * (p.d / kFp8Group) + nt]);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) sum[i][0] += sc * acc[i][0];
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          sum[i][0][c] = own ? fmaf(sc, acc[i][0][c], sum[i][0][c]) : sum[i][0][c];
     }
     u += k1 - k0;
   }
