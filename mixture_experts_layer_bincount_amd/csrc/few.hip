@@ -118,10 +118,10 @@ __global__ __launch_bounds__(kRouterWaves * 64) void few_router_kernel(
       bf16x8 pl[3];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t h = f32_to_bf16_bits(v[i]);
+        const uint32_t h = f32_to_bf16_bits_any(v[i]);
         const float r1 = v[i] - bf16_bits_to_f32(h);
-        const uint32_t m = f32_to_bf16_bits(r1);
-        const uint32_t l = f32_to_bf16_bits(r1 - bf16_bits_to_f32(m));
+        const uint32_t m = f32_to_bf16_bits_any(r1);
+        const uint32_t l = f32_to_bf16_bits_any(r1 - bf16_bits_to_f32(m));
         pl[0][i] = __builtin_bit_cast(__bf16, (uint16_t)h);
         pl[1][i] = __builtin_bit_cast(__bf16, (uint16_t)m);
         pl[2][i] = __builtin_bit_cast(__bf16, (uint16_t)l);
@@ -556,12 +556,8 @@ __device__ __forceinline__ void gate_up_items(const FewParams& p, const FewLds& 
       ga *= sc1;
       up *= sc3;
       const float h = ga / (1.f + __expf(-ga)) * up * wgt;
-      // three bf16 terms (a value past bf16's range keeps its first term)
-      const uint32_t hb = f32_to_bf16_bits(h);
-      float rest = h - bf16_bits_to_f32(hb);
-      if ((hb & 0x7F80u) == 0x7F80u) rest = 0.f;
-      const uint32_t mb = f32_to_bf16_bits(rest);
-      const uint32_t lb = f32_to_bf16_bits(rest - bf16_bits_to_f32(mb));
+      uint32_t hb, mb, lb;
+      split3(h, hb, mb, lb);
       // two neighbouring columns per store, by the even lane
       const uint32_t hv = hb | (uint32_t)__shfl_xor((int)hb, 1, 64) << 16;
       const uint32_t mv = mb | (uint32_t)__shfl_xor((int)mb, 1, 64) << 16;

@@ -25,6 +25,11 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
   uint32_t u = __float_as_uint(f);
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
+// The same for any value: a NaN of any bits is a NaN (as a number, one whose fraction is
+// all ones would carry out of the exponent and come out as a zero).
+__device__ __forceinline__ uint32_t f32_to_bf16_bits_any(float f) {
+  return f == f ? f32_to_bf16_bits(f) : 0x7FC0u;
+}
 
 constexpr int kMaxDevices = 64;  // devices whose launch facts are cached
 

@@ -94,11 +94,11 @@ __global__ __launch_bounds__(256) void router_split_kernel(const float* __restri
     const int e = (int)(i / d);
     const int k = (int)(i % d);
     const float w = (e < E) ? W_g[(int64_t)k * E + e] : 0.f;
-    const uint32_t h = f32_to_bf16_bits(w);
+    const uint32_t h = f32_to_bf16_bits_any(w);
     const float r1 = w - bf16_bits_to_f32(h);
-    const uint32_t m = f32_to_bf16_bits(r1);
+    const uint32_t m = f32_to_bf16_bits_any(r1);
     const float r2 = r1 - bf16_bits_to_f32(m);
-    const uint32_t l = f32_to_bf16_bits(r2);
+    const uint32_t l = f32_to_bf16_bits_any(r2);
     Wp[i] = (uint16_t)h;
     Wp[n + i] = (uint16_t)m;
     Wp[2 * n + i] = (uint16_t)l;

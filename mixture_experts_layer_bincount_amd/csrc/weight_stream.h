@@ -124,10 +124,10 @@ __device__ __forceinline__ bf16x8 widen(const u32x4& q, int i) {
   }
 }
 
-// Three bf16 terms of a value (24 bits; a value past bf16's range keeps its
-// first term).
+// Three bf16 terms of a value (24 bits; NaN and a value past bf16's range keep
+// their first term).
 __device__ __forceinline__ void split3(float v, uint32_t& h, uint32_t& m, uint32_t& l) {
-  h = f32_to_bf16_bits(v);
+  h = f32_to_bf16_bits_any(v);
   float rest = v - bf16_bits_to_f32(h);
   if ((h & 0x7F80u) == 0x7F80u) rest = 0.f;
   m = f32_to_bf16_bits(rest);
