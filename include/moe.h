@@ -354,11 +354,13 @@ size_t moe_few_workspace_bytes(const moe_shape* shape);
  * where the layer is the stream of the touched experts' weights and
  * moe_forward's launches and row tiles cost as much again.  Up to 16 tokens take two
  * launches (route; select, group, gate/up, down and combine), more take moe_forward's
- * route, dispatch and grouped combine with two launches of the experts between.  It is the faster call
- * for narrow experts and for quantised weights (one token, 64 experts of 1408: 39 us
- * against 110; 16 tokens, Mixtral-shaped, int4: 239 against 241); wide bf16 experts
- * are read faster by moe_forward (one token 143 us against 152, 16 tokens 459
- * against 570, 64 tokens 471 against 775).
+ * route, dispatch and grouped combine with two launches of the experts between.
+ * Up to 16 tokens it is the faster call for narrow experts and mostly for quantised
+ * weights (one token, 64 experts of 1408: 39 us against 113; 16 tokens, Mixtral-shaped,
+ * int4: 235 against 243); wide bf16 experts are read faster by moe_forward (16 tokens
+ * 480 us against 548).  From 17 tokens on moe_forward is faster for nearly all weights
+ * (64 tokens, Mixtral-shaped: bf16 492 us against 763, int4 262 against 426), and what
+ * this call has over it is fp32's precision of the hidden activation and equal bits.
  *   - SwiGLU experts in every weight type, group-limited routing, a shared
  *     expert, the capacity with MOE_OVERFLOW_DROP and MOE_OVERFLOW_SHARED.
  *     MOE_ERR_UNSUPPORTED: more tokens, Linear+bias experts,
@@ -368,6 +370,8 @@ size_t moe_few_workspace_bytes(const moe_shape* shape);
  *   - The hidden activation keeps fp32's precision (three bf16 terms) and a
  *     token's experts are summed in a fixed order: equal calls give equal
  *     bits.  shape->hidden_split and shape->combine change nothing here.
+ *   - A token depends on its own experts only: infinities and NaN in the weights
+ *     of others, or in other tokens, do not reach it.
  *   - Expert matrices are 16-byte aligned in every weight type; with quantised
  *     weights d is a multiple of 128 (one scale per 128 rows of W2).
  *   - ws [device] holds moe_few_workspace_bytes(shape) bytes, 256-byte aligned;
@@ -419,7 +423,9 @@ size_t moe_adapter_workspace_bytes(const moe_adapter_shape* shape);
  * so that, for a served block: the attention output's projection with every
  * request's adapter, in front of the layer (y bf16), or adapters in parallel to
  * the layer, added to its fp32 output (W NULL, base = y).
- *   - Rows in any order; adapters may have no row, one or all.
+ *   - Rows in any order; adapters may have no row, one or all.  Past 64 rows, rows of
+ *     many adapters are faster in runs of one adapter than scattered (4096 rows, 64
+ *     adapters of rank 16 / 128, 4096 -> 4096: 157 / 293 us against 341 / 1600).
  *   - All sums are fp32; x A^T is not rounded to fewer than 24 bits before B.
  *     y is rounded once.  Equal calls give equal bits.
  *   - A row depends on its own adapter only: infinities and NaN in another

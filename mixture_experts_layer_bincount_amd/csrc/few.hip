@@ -27,6 +27,14 @@
 // into h, h is kept in three bf16 terms (24 bits: as exact as fp32, and bf16
 // MFMA time is free here), and the k pieces of a row of y are added in order,
 // so results do not depend on timing: equal calls give equal bits.
+//
+// Loop control is scalar throughout: tickets, segments, steps and what waits compare
+// pass through uniform() wherever they come from LDS or memory, and no loop that lanes
+// leave one by one keeps values alive that are used after it.  This is not for speed.
+// A form with such values in vector registers was compiled with the copy of a live
+// one placed at the end of a divergent loop, where the execution mask is still empty:
+// the copy wrote nothing, the item count came back as what the register had held, and
+// tickets past the last item were worked on at addresses out of range.
 #include <algorithm>
 
 #include "moe_internal.h"

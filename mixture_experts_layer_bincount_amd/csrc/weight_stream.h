@@ -173,11 +173,13 @@ struct StepMap {
 
 // A wave's share of the steps [begin, end) of a row: of every W consecutive
 // pairs (or steps) one, so that the W waves of a workgroup read a row's
-// consecutive lines at about the same time (DRAM pages stay open: see the
-// kernels for what that measured).
+// consecutive lines at about the same time and DRAM pages stay open (one token,
+// Mixtral widths, gate/up items by their time stamps: 6.4 TB/s, against 5.4 with a
+// part of the row for each wave).
 // The walk starts `turn` (a row tile's own number) into the share: row tiles
 // that are streamed at the same time are whole rows apart, and at equal k many
-// of their lines would lie in the same memory channels.
+// of their lines would lie in the same memory channels.  (The down items' rate was
+// the same without it.)
 struct StepShare {
   int begin, end, count, stride, pair, start;
   __device__ __forceinline__ StepShare(int b, int e, int wave, int W, int pr, int turn) {
