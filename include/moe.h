@@ -371,7 +371,9 @@ size_t moe_few_workspace_bytes(const moe_shape* shape);
  *     token's experts are summed in a fixed order: equal calls give equal
  *     bits.  shape->hidden_split and shape->combine change nothing here.
  *   - A token depends on its own experts only: infinities and NaN in the weights
- *     of others, or in other tokens, do not reach it.
+ *     of others, or in other tokens, do not reach it (a token of NaN still takes its
+ *     place in the experts' capacity).  An infinite weight of its own expert may come
+ *     out as NaN: it meets the three terms one by one.
  *   - Expert matrices are 16-byte aligned in every weight type; with quantised
  *     weights d is a multiple of 128 (one scale per 128 rows of W2).
  *   - ws [device] holds moe_few_workspace_bytes(shape) bytes, 256-byte aligned;
@@ -429,7 +431,8 @@ size_t moe_adapter_workspace_bytes(const moe_adapter_shape* shape);
  *   - All sums are fp32; x A^T is not rounded to fewer than 24 bits before B.
  *     y is rounded once.  Equal calls give equal bits.
  *   - A row depends on its own adapter only: infinities and NaN in another
- *     row or another adapter do not reach it.
+ *     row or another adapter do not reach it (infinities of its own may come out as
+ *     NaN).
  *   - x, W, A and B are 16-byte aligned, ws 256-byte.
  *   - ws [device] holds moe_adapter_workspace_bytes(shape) bytes; nothing in it
  *     outlives the call.  Calls that share a workspace must not overlap.
