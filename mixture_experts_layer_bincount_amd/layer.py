@@ -84,6 +84,8 @@ class MoELayer:
             ranks = adapters.get("ranks")
             if ranks is not None and (tuple(ranks.shape) != (n,) or ranks.dtype != torch.int32):
                 raise ValueError("adapters: ranks is int32 [n]")
+            if any(t is not None and t.device.type != dev.type for t in adapters.values()):
+                raise ValueError(f"adapters: the tensors lie on the layer's device ({dev.type})")
             self.adapters = dict(adapters)
             self.adapter_shape = make_adapter_shape(T, d, d, n, rank, y_dtype=DT_F32)
             self.adapter_ws = adapter_workspace(self.adapter_shape, dev)
@@ -94,6 +96,8 @@ class MoELayer:
                 raise ValueError("adapter_idx needs a layer with adapters")
             if tuple(adapter_idx.shape) != (self.shape.T,) or adapter_idx.dtype != torch.int32:
                 raise ValueError("adapter_idx is int32 [T]")
+            if adapter_idx.device.type != self.y.device.type:
+                raise ValueError("adapter_idx lies on the layer's device")
         W_g = self.W_g_packed if self.W_g_packed is not None else self.W_g
         forward = moe_forward_few if self.few else moe_forward
         forward(self.shape, x, W_g, self.b_g, self.weights, self.y, self.topk_idx,

@@ -1,4 +1,4 @@
-"""moe_adapter_workspace_bytes on the host: empty batches."""
+"""moe_adapter_workspace_bytes on the host, and what a layer with adapters refuses there."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -48,3 +48,22 @@ def test_workspace_serves_smaller_batches(moe, kw):
     assert got[0] > 0
     down = [(a, b) for a, b, x, y in zip(rows, rows[1:], got, got[1:]) if y < x]
     assert not down, down[:5]
+
+
+def test_layer_refuses_adapters_of_another_device(moe):
+    """A kernel would follow their addresses."""
+    ok = dict(A=torch.zeros(2, 16, 64, dtype=torch.bfloat16),
+              B=torch.zeros(2, 64, 16, dtype=torch.bfloat16), scales=torch.zeros(2),
+              ranks=torch.zeros(2, dtype=torch.int32))
+
+    def layer(**kw):
+        return moe.MoELayer(3, 64, 4, 2, 128, W_g=None, weights={}, device="cpu",
+                            pack_router=False, adapters={**ok, **kw})
+
+    for name in ok:
+        with pytest.raises(ValueError, match="device"):
+            layer(**{name: ok[name].to("meta")})
+    with pytest.raises(ValueError, match="device"):
+        layer()(torch.zeros(3, 64, dtype=torch.bfloat16),
+                adapter_idx=torch.zeros(3, dtype=torch.int32, device="meta"))
+    assert layer(ranks=None).adapters["ranks"] is None
